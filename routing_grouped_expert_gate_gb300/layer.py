@@ -244,7 +244,8 @@ def quantize_experts(p: Dict[str, Optional[torch.Tensor]], group: int = 128,
 def alloc_decode_buffers(cfg, device, norm: bool = False, rows8: bool = False,
                          alloc=None) -> Dict[str, torch.Tensor]:
     """The buffers of one decode; with `rows8` (which needs the norm) the experts
-    read the norm's 8-bit output."""
+    read the norm's 8-bit output. Parameters without the norm's weight may use
+    them too: the experts then read x itself."""
     if rows8 and not norm:
         raise ValueError("8-bit rows come from the norm")
     T, d, E, k = cfg.T, cfg.d, cfg.E, cfg.k
@@ -276,13 +277,15 @@ def decode(cfg, p: Dict[str, object], x: torch.Tensor, b: Dict[str, torch.Tensor
     themselves, and no aux loss is formed."""
     T, k, E, F, Fs = cfg.T, cfg.k, cfg.E, cfg.F, cfg.F_shared
     ws, group = b["ws"], p["group"]
+    rows, scale = x, None
     if p.get("w_norm") is not None:
         L.add_rmsnorm(cfg, x, residual, p["w_norm"], norm_eps, b["sum"], b["x_norm"],
                       b.get("x8"), b.get("x8_scale"), None, stream)
-        x = b["x_norm"]
+        rows = x = b["x_norm"]
+        if b.get("x8") is not None:
+            rows, scale = b["x8"], b["x8_scale"]
     elif residual is not None:
         raise ValueError("a residual needs the norm's weight w_norm")
-    rows, scale = (x, None) if b.get("x8") is None else (b["x8"], b["x8_scale"])
     L.route_topk(cfg, x, p["w_router"], p.get("logit_bias"), p.get("sel_bias"), b["logits"],
                  b["idx"], b["w"], ws, stream)
     L.permute(cfg, None, b["idx"], b["counts"], b["offsets"], b["row_of"], b["src_tok"], None, ws,
