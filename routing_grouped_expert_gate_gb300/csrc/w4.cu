@@ -10,12 +10,12 @@
 // shared or tensor memory first, four times the codes' bytes, and its
 // accumulators back after every scale group.
 //
-// What bounds it in the end is the arithmetic pipe that decodes: seven
+// What it spends its time on beside the loads is the decoding: eleven
 // instructions per eight codes, (word >> 4 i) & 0x000f000f | 0x43004300 being a
-// pair of bf16 128 + u. The 136 too much per code is taken off exactly, or per
-// scale group (W4::kExact). The products of a scale group are summed in fp32 by
-// the tensor cores, then multiplied by the group's scale and added in fp32: the
-// weights themselves are never rounded.
+// pair of bf16 128 + u and a packed subtraction of 136 making it u - 8, exactly.
+// The products of a scale group are summed in fp32 by the tensor cores, then
+// multiplied by the group's scale and added in fp32: the weights themselves are
+// never rounded.
 //
 // The code layout makes a lane's 16-byte load hold its operands of four
 // consecutive 32-k blocks: within 128 k, the word at position 4 t + j holds k
@@ -23,11 +23,11 @@
 // 8 t .. 8 t + 7, and the matching activations are 16 consecutive bytes.
 //
 // Measured (GB300, all launches of a call): one token through 2 of 8 experts of
-// 4096 x 14336, groups of 128: 51 us, 3.6 TB/s (82 us with codes straight to
+// 4096 x 14336, groups of 128: 50 us, 3.6 TB/s (82 us with codes straight to
 // registers and one slab ahead); 12 tokens, 8 of 64 experts of 2048 x 1408 each,
-// groups of 32: 66 us, 3.8 TB/s; 64 tokens, 2 of 8 wide experts, groups of 64:
+// groups of 32: 65 us, 3.8 TB/s; 64 tokens, 2 of 8 wide experts, groups of 64:
 // 218 us, 3.4 TB/s. With the arithmetic left out the same loads take 36, 47 and
-// 125 us; with the loads left out the arithmetic takes 42, 51 and 200 us.
+// 125 us.
 #include "common.cuh"
 #include "internal.h"
 #include "mx8.cuh"

@@ -14,21 +14,14 @@ namespace moe {
 
 namespace {
 
-// d = a b + c
-__device__ __forceinline__ void mma_onto(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1, const float (&c)[4]) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
-        "f"(c[2]), "f"(c[3]));
-}
 // d = a b
 __device__ __forceinline__ void mma_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
-  const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-  mma_onto(d, a, b0, b1, zero);
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // c += a b
 __device__ __forceinline__ void mma_add(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -40,14 +33,16 @@ __device__ __forceinline__ void mma_add(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Bits 4i..4i+3 of both halves of w as a pair of bf16: 128 + u, or (EXACT) u -
-// 8. (x & mask) | magic is one instruction when only one of the two constants
-// is an immediate, so the mask comes in a register.
-template <bool EXACT>
+// Bits 4i..4i+3 of both halves of w as a pair of bf16 u - 8, exactly: 128 + u
+// by bits, less 136. (x & mask) | magic is one instruction when only one of the
+// two constants is an immediate, so the mask comes in a register. Taking 136
+// sum_k x[k] off a group's sum of (128 + u) x instead leaves the rounding of 136
+// |x| in it, whatever the weight, and is no faster: one token through 2 of 8
+// experts of 4096 x 14336 50.8 us (50.0 so), 12 tokens through 8 of 64 of 2048 x
+// 1408 66.4 us (64.7).
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i, uint32_t mask) {
   uint32_t t;
   asm("lop3.b32 %0, %1, %2, 0x43004300, 0xEA;" : "=r"(t) : "r"(w >> (4 * i)), "r"(mask));
-  if (!EXACT) return t;
   const uint32_t k136 = 0x43084308u;
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&t),
                                    *reinterpret_cast<const __nv_bfloat162*>(&k136));
@@ -190,15 +185,6 @@ struct W4 {
   using S = Shape<NTMAX, HOW>;
   using Out = typename std::conditional<P == 3, float, bf16>::type;
   static constexpr int kMt = S::kMt;
-  // The codes enter the products as 128 + u, and 136 sum_k x[k] is taken off
-  // again: -136 in every place of an A operand gives it for all rows at once,
-  // which two tiles share. That is cheaper than subtracting 136 from each pair
-  // of codes (4 products per 32 k against 32 subtractions). A group's sum then
-  // starts at up to 136 sum |x| and takes at most 18 additions of at most one
-  // step of 2^-23 each: it is off by under 2^-11 code steps per weight, where
-  // the 4-bit codes themselves stand for half a step. Where a warp has one
-  // tile, or the rows are fp32, the codes are made exact instead.
-  static constexpr bool kExact = P == 3 || NTMAX > 1;
   // activations of a stage: per plane a box of four pieces of 64 k (128 bytes,
   // 128-byte swizzle) of all a unit's rows (of eight for a unit with no more)
   static constexpr int kBoxX = NTMAX * 1024, kPlaneX = 4 * kBoxX, kX = P * kPlaneX;
@@ -435,19 +421,7 @@ struct W4 {
       // k 32 j + 8 tig of the slab: piece 4 (j & 1) + tig of a row in the slab's
       // box j / 2, at its place xor the row mod 8
       constexpr int kBox = NT == 1 ? 1024 : kBoxX;
-      float part[kMt][NT][4], base[4];
-      uint4 b1[J];
-      if (!kExact) {  // one token tile, one plane: -136 times the group's sums
-        const uint32_t k136[4] = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
-#pragma unroll
-        for (int jj = 0; jj < J; ++jj) {
-          const int j = g * J + jj;
-          b1[jj] = *reinterpret_cast<const uint4*>(x + (j >> 1) * kBox + ((j & 1) ? flip : 0));
-          if (jj == 0) mma_new(base, k136, b1[0].x, b1[0].y);
-          else mma_add(base, k136, b1[jj].x, b1[jj].y);
-          mma_add(base, k136, b1[jj].z, b1[jj].w);
-        }
-      }
+      float part[kMt][NT][4];
 #pragma unroll
       for (int jj = 0; jj < J; ++jj) {
         const int j = g * J + jj;
@@ -459,22 +433,21 @@ struct W4 {
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              a0[m][2 * i + h] = code_pair<kExact>(word_of(w[m][h], j), i, mask);
-              a1[m][2 * i + h] = code_pair<kExact>(word_of(w[m][h], j), 2 + i, mask);
+              a0[m][2 * i + h] = code_pair(word_of(w[m][h], j), i, mask);
+              a1[m][2 * i + h] = code_pair(word_of(w[m][h], j), 2 + i, mask);
             }
 #pragma unroll
         for (int p = P - 1; p >= 0; --p) {  // the smallest plane first
           uint4 b[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            b[n] = kExact ? *reinterpret_cast<const uint4*>(xj + p * kPlaneX + n * 1024) : b1[jj];
+            b[n] = *reinterpret_cast<const uint4*>(xj + p * kPlaneX + n * 1024);
           const bool begins = jj == 0 && p == P - 1;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int m = 0; m < kMt; ++m) {
-              if (begins && !kExact) mma_onto(part[m][n], a0[m], b[n].x, b[n].y, base);
-              else if (begins) mma_new(part[m][n], a0[m], b[n].x, b[n].y);
+              if (begins) mma_new(part[m][n], a0[m], b[n].x, b[n].y);
               else mma_add(part[m][n], a0[m], b[n].x, b[n].y);
             }
 #pragma unroll
