@@ -645,12 +645,19 @@ struct W4 {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) __stcg(slot + mine + (n * 4 + i) * 32, acc[0][n][i]);
-      __threadfence();
+      // Lane 0's fences stand between the warp's barriers and its ticket, so that
+      // the ticket releases what all lanes stored and a ticket that is the last
+      // one acquires it for all lanes.
       __syncwarp();
       uint32_t before = 0;
-      if (lane == 0) before = atomicAdd(a.came + lo * S::kTiles + tile, 1u);
-      if (__shfl_sync(0xffffffffu, before, 0) != hi - lo) return;
-      __threadfence();
+      if (lane == 0) {
+        __threadfence();
+        before = atomicAdd(a.came + lo * S::kTiles + tile, 1u);
+        __threadfence();
+      }
+      before = __shfl_sync(0xffffffffu, before, 0);
+      __syncwarp();
+      if (before != hi - lo) return;
       for (uint32_t b = lo; b <= hi; ++b) {
         const float* q = a.part + ((int64_t)b * 2 + (b == lo)) * S::kPart + mine;
 #pragma unroll
