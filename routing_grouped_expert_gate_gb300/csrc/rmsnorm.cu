@@ -12,6 +12,7 @@
 // (16000 x 512: 13.4 us, 14.1 with a block), a block above (16000 x 1000 fp32:
 // 43 us, 52 with a warp).
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -508,14 +509,15 @@ cudaError_t fwd(const Ctx& c, const NormFwd& a) {
 template <typename T, int C, int R, int THREADS, int BLOCKS>
 cudaError_t launch_ring(const Ctx& c, const NormBwd& a, const BwdShape& s, int blocks) {
   auto kern = rmsnorm_bwd_ring<T, C, R, THREADS, BLOCKS>;
-  static bool attr_done[64];
+  static std::atomic<uint64_t> attr_set_mask{0};  // bit: device
   int dev = 0;
   cudaGetDevice(&dev);
-  if (!attr_done[dev & 63]) {
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_set_mask.load() & bit)) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     if (e != cudaSuccess) return e;
-    attr_done[dev & 63] = true;
+    attr_set_mask.fetch_or(bit);
   }
   const int row_bytes = a.d * (int)sizeof(T), stage = (a.d_sum != nullptr ? 3 : 2) * R * row_bytes;
   const NormRing r{a, std::min(kMaxRing, kRingBytes / s.per_sm / stage), row_bytes, c.status,

@@ -2,6 +2,7 @@
 // codes are laid out), instantiated for one group size per file.
 #pragma once
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -851,13 +852,14 @@ constexpr int kMostShared = 222 * 1024;
 
 template <bool FIRST, int NTMAX, int P, int GS, Sharing HOW>
 cudaError_t allow_shared() {
-  static bool done[64];
+  static std::atomic<uint64_t> attr_set_mask{0};  // bit: device
   int dev = 0;
   cudaGetDevice(&dev);
-  if (done[dev & 63]) return cudaSuccess;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (attr_set_mask.load() & bit) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(w4_product<FIRST, NTMAX, P, GS, HOW>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
-  done[dev & 63] = e == cudaSuccess;
+  if (e == cudaSuccess) attr_set_mask.fetch_or(bit);
   return e;
 }
 
@@ -883,10 +885,11 @@ cudaLaunchConfig_t config(int blocks, int threads, size_t shared, cudaStream_t s
 // all of them.
 template <bool FIRST, int NTMAX, int P, int GS>
 int places(const Ctx& c, int split) {
-  static int known[64][9];
+  static std::atomic<int> known[64][9];  // one more than the number; 0: not asked yet
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
-  if (known[dev & 63][split] != 0) return known[dev & 63][split];
+  const int got = known[dev & 63][split].load();
+  if (got != 0) return got - 1;
   constexpr Sharing kHow = NTMAX == 1 ? Sharing::kLate : Sharing::kInTurn;
   if (allow_shared<FIRST, NTMAX, P, GS, kHow>() != cudaSuccess) return 0;
   cudaLaunchAttribute attr[2];
@@ -896,7 +899,8 @@ int places(const Ctx& c, int split) {
     cudaGetLastError();
     return 0;
   }
-  return known[dev & 63][split] = n;
+  known[dev & 63][split].store(n + 1);
+  return n;
 }
 
 // How the blocks share the tasks. Whole tasks in turn (split 1); or clusters of
