@@ -288,7 +288,11 @@ __device__ __forceinline__ float sum_of(const float* red, int warps) {
   return v;
 }
 
-// R rows at a time share one barrier, and few blocks leave few partial sums.
+// R rows at a time share one barrier, and few blocks leave few partial sums. Where
+// R rows a block would leave SMs without one, fewer: 300 x 4096 bf16 6.0 us with
+// two rows, 6.7 with three; 16 x 4096 4.1 with one, 5.1 with three. A block holds
+// no more stages than it has rounds, so that the column sums' blocks find room
+// next to few rows' (300 x 2048 fp32 5.4 us, 6.0 with all stages).
 // 16000 x 1000 bf16: 25 us with three rows and three blocks an SM, 27 with two
 // and six, 36 with one (and 47 with a warp a row and no ring); 4096 x 4096 bf16
 // 25.5 us with three and one block, 27.7 with two and two, 30 with one; fp32 45
@@ -461,6 +465,9 @@ __global__ void __launch_bounds__(256) rmsnorm_zero(float* dw, int d) {
   if (j < d) dw[j] = 0.f;
 }
 
+constexpr int kMostSms = 256;  // the workspace is sized without a device
+int device_sms(const Ctx& c) { return std::min(c.sm_count, kMostSms); }
+
 // threads of a row-per-block kernel with C chunks of 8 per thread
 int row_threads(int d, int C) {
   const int n = (d / 8 + C - 1) / C;
@@ -470,26 +477,33 @@ int row_threads(int d, int C) {
 constexpr int kWarpRowD = 512;  // up to here a warp holds a row (two chunks a lane)
 constexpr int kWarpsPerBlock = 8;
 
-// The backward's shape for a width: rows at a time, threads of a block and
-// blocks on an SM.
+// The backward's shape for a size: rows at a time, chunks of eight elements and
+// threads of a block, blocks on an SM.
 struct BwdShape {
-  int rows, threads, per_sm;
+  int rows, chunks, threads, per_sm;
 };
-BwdShape bwd_shape(int d, int act_dtype) {
-  if (d <= kWarpRowD) return {kWarpsPerBlock, 32 * kWarpsPerBlock, 4};
-  if (d > 8192) return {1, row_threads(d, 2), 1};
+BwdShape bwd_shape(int64_t T, int d, int act_dtype, int sms) {
+  if (d <= kWarpRowD) return {kWarpsPerBlock, d <= 256 ? 1 : 2, 32 * kWarpsPerBlock, 4};
+  if (d > 8192) return {1, 2, row_threads(d, 2), 1};
   const int es = act_dtype == MOE_BF16 ? 2 : 4;
-  BwdShape s = d <= 1024   ? BwdShape{3, row_threads(d, 1), 3}
-               : d <= 2048 ? BwdShape{3, row_threads(d, 1), es == 2 ? 2 : 1}
-               : d <= 4096 ? BwdShape{es == 2 ? 3 : 2, row_threads(d, 1), 1}
-                           : BwdShape{1, row_threads(d, 2), 1};
+  BwdShape s = d <= 1024   ? BwdShape{3, 1, 0, 3}
+               : d <= 2048 ? BwdShape{3, 1, 0, es == 2 ? 2 : 1}
+               : d <= 4096 ? BwdShape{es == 2 ? 3 : 2, 1, 0, 1}
+                           : BwdShape{1, 2, 0, 1};
+  // no more rows at a time than give every SM a block
+  s.rows = (int)std::max<int64_t>(1, std::min<int64_t>(s.rows, (T + sms - 1) / sms));
+  // A block of 512 threads leaves the column sums' blocks no registers. With one
+  // round a block it pays to start them early: half as many threads (200 x 4096
+  // bf16 5.6 us, 6.2 with 512; fp32 gains nothing).
+  if (es == 2 && d > 2048 && T <= 2 * (int64_t)sms) s.chunks = 2;
+  s.threads = row_threads(d, s.chunks);
   // two stages of three inputs for each block, or fewer blocks
   s.per_sm = std::max(1, std::min(s.per_sm, kRingBytes / (6 * s.rows * d * es)));
   return s;
 }
 
 int bwd_blocks(const moe_cfg& cfg, int sms) {
-  const BwdShape s = bwd_shape(cfg.d, cfg.act_dtype);
+  const BwdShape s = bwd_shape(cfg.T, cfg.d, cfg.act_dtype, sms);
   return (int)std::min<int64_t>((cfg.T + s.rows - 1) / s.rows, (int64_t)s.per_sm * sms);
 }
 
@@ -520,24 +534,35 @@ cudaError_t launch_ring(const Ctx& c, const NormBwd& a, const BwdShape& s, int b
     attr_set_mask.fetch_or(bit);
   }
   const int row_bytes = a.d * (int)sizeof(T), stage = (a.d_sum != nullptr ? 3 : 2) * R * row_bytes;
-  const NormRing r{a, std::min(kMaxRing, kRingBytes / s.per_sm / stage), row_bytes, c.status,
-                   c.timeout_ns};
+  const int64_t rounds = (a.T + (int64_t)R * blocks - 1) / ((int64_t)R * blocks);
+  const int stages = (int)std::min<int64_t>(rounds, std::min(kMaxRing, kRingBytes / s.per_sm / stage));
+  const NormRing r{a, stages, row_bytes, c.status, c.timeout_ns};
   return launch_dependent(kern, dim3(blocks), dim3(s.threads), (size_t)r.stages * stage, c.stream, r);
+}
+
+// up to R rows at a time
+template <typename T, int C, int R, int THREADS, int BLOCKS>
+cudaError_t launch_rows(const Ctx& c, const NormBwd& a, const BwdShape& s, int blocks) {
+  if (s.rows == 1) return launch_ring<T, C, 1, THREADS, BLOCKS>(c, a, s, blocks);
+  if (R == 2 || s.rows == 2) return launch_ring<T, C, 2, THREADS, BLOCKS>(c, a, s, blocks);
+  return launch_ring<T, C, R, THREADS, BLOCKS>(c, a, s, blocks);
 }
 
 template <typename T>
 cudaError_t bwd(const Ctx& c, const NormBwd& a, int blocks) {
-  const BwdShape s = bwd_shape(a.d, sizeof(T) == 2 ? MOE_BF16 : MOE_F32);
+  constexpr bool kHalf = sizeof(T) == 2;
+  const BwdShape s = bwd_shape(a.T, a.d, kHalf ? MOE_BF16 : MOE_F32, device_sms(c));
   if (a.d <= kWarpRowD) {
     const dim3 g(blocks), b(s.threads);
     const size_t sm = (size_t)a.d * sizeof(float);
     if (a.d <= 256) return launch_dependent(rmsnorm_bwd<T, 1, true, 256>, g, b, sm, c.stream, a);
     return launch_dependent(rmsnorm_bwd<T, 2, true, 256>, g, b, sm, c.stream, a);
   }
-  constexpr bool kHalf = sizeof(T) == 2;
-  if (a.d <= 1024) return launch_ring<T, 1, 3, 128, 3>(c, a, s, blocks);
-  if (a.d <= 2048) return launch_ring<T, 1, 3, 256, kHalf ? 2 : 1>(c, a, s, blocks);
-  if (a.d <= 4096) return launch_ring<T, 1, kHalf ? 3 : 2, 512, 1>(c, a, s, blocks);
+  if (a.d <= 1024) return launch_rows<T, 1, 3, 128, 3>(c, a, s, blocks);
+  if (a.d <= 2048) return launch_rows<T, 1, 3, 256, kHalf ? 2 : 1>(c, a, s, blocks);
+  if constexpr (kHalf)
+    if (a.d <= 4096 && s.chunks == 2) return launch_rows<T, 2, 2, 256, 2>(c, a, s, blocks);
+  if (a.d <= 4096) return launch_rows<T, 1, kHalf ? 3 : 2, 512, 1>(c, a, s, blocks);
   if (a.d <= 8192) return launch_ring<T, 2, 1, 512, 1>(c, a, s, blocks);
   return launch_dependent(rmsnorm_bwd<T, 2, false, 1024>, dim3(blocks), dim3(s.threads), 0,
                           c.stream, a);
@@ -552,8 +577,6 @@ cudaError_t launch_add_rmsnorm(const Ctx& c, const moe_cfg& cfg, const void* x, 
   return cfg.act_dtype == MOE_BF16 ? fwd<bf16>(c, a) : fwd<float>(c, a);
 }
 
-constexpr int kMostSms = 256;  // the workspace is sized without a device
-
 size_t rmsnorm_bwd_ws_bytes(const moe_cfg& cfg) {
   return (size_t)bwd_blocks(cfg, kMostSms) * cfg.d * sizeof(float);
 }
@@ -566,7 +589,7 @@ cudaError_t launch_add_rmsnorm_bwd(const Ctx& c, const moe_cfg& cfg, const void*
     note_launches(1);
     return cudaGetLastError();
   }
-  const int blocks = bwd_blocks(cfg, c.sm_count < kMostSms ? c.sm_count : kMostSms);
+  const int blocks = bwd_blocks(cfg, device_sms(c));
   NormBwd a{dy, d_sum, sum, w, rstd, dx, static_cast<float*>(ws), 1.f / (float)cfg.d, cfg.T, cfg.d};
   cudaError_t e = cfg.act_dtype == MOE_BF16 ? bwd<bf16>(c, a, blocks) : bwd<float>(c, a, blocks);
   if (e != cudaSuccess) return e;
