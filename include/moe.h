@@ -578,7 +578,8 @@ int moe_w4_grouped_swiglu(const moe_cfg* cfg, int32_t n_groups, int64_t n_rows, 
  *   m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
  *   p = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
  * in fp32 (m and v with one rounding per product and sum), then step[0] = t.
- * Each element is read and written once; one launch takes 96 tensors.
+ * Each element is read and written once; one launch takes 96 tensors with
+ * states of one size.
  *   p       MOE_BF16 or MOE_F32 parameters, updated; with `master` (fp32, for
  *           bf16 p only) the update runs on the master copy and p is its rounding
  *           (without one, a step below half of p's last bit leaves p as it is)

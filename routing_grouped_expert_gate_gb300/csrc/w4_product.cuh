@@ -126,8 +126,8 @@ constexpr int kMaxStages = 8;
 // blocks whose sums meet in its shared memory.
 // Late (one token tile, clusters): and a task's outputs are finished one task
 // late, with one more warp that tells the other blocks of a block's sums (one
-// token, 2 of 8 wide experts: 50 us, 53 in turn; in blocks of their own it only
-// cost: 12 tokens on 64 experts 73 us, 69 in turn).
+// token, 2 of 8 wide experts: 50 us, 85 with whole tasks in turn; in blocks of
+// their own it only costs: 12 tokens on 64 experts 66 us, 65 in turn).
 // Dealt (more token tiles): the steps of all tasks, in a row, in even parts by
 // their time, so that a task may begin in one block and end in another; their
 // sums meet in global memory. That fills all blocks, whatever the number of
@@ -259,7 +259,9 @@ struct W4 {
     pairs = (a.S + 1) / 2;
     in_unit = (uint64_t)per * pairs;
     total = sh.prew[a.G] * in_unit;
-    // two steps for a block at least
+    // As many blocks as leave each one step at least, whatever the steps' weights
+    // (total / nblk is at least a full unit's step). The count of those that share a
+    // task relies on it: no block between the first and the last may be without a step.
     nblk = (uint32_t)min((uint64_t)gridDim.x, quotient(total, 2 * step_weight(8 * NTMAX)) + 1);
     const bool any = total > 0 && blockIdx.x < nblk;
     const int64_t at = any ? first_step(blockIdx.x) : 0;
